@@ -40,10 +40,19 @@
 //   S[t, h]  = sum_g scale[t, g] (codes_g . q_h) + zero[t, g] (sum of q_h over g)
 //   O[d, h]  = sum_t (p[t, h] scale[t, g(d)]) code[t, d] + sum_t p[t, h] zero[t, g(d)]
 // the scores' scales in fp32 on the accumulators, the output's as one scaled
-// copy of P per group (P is rounded to fp16: 2^-11 relative at most, against
-// bf16's 2^-8); the zeros as one more product each, whose small operand is the
-// zeros as they lie in the parameter rows (the sums of q in two fp16 parts,
-// so that 22 bits of them take part).
+// copy of P per group; the zeros as one more product each, whose small operand
+// is the zeros as they lie in the parameter rows (the sums of q in two fp16
+// parts, so that 22 bits of them take part).
+//
+// P and P scale are fp16, rounded by 2^-11 (against bf16's 2^-8) as long as they
+// are no subnormals.  Small values under a row with most of the weight would make
+// them such: then their codes lose their weight while their zeros and l keep it,
+// and the row stands for its groups' least values.  So P is formed as 2^14 times
+// the weight (o, oz and l alike, which cancels at the end), and a group's scales
+// are taken over a bound, the least power of two from 2^-14 to 2^14 that no scale
+// the warp has met exceeds; where it has to grow the sums so far are rescaled.  A
+// subnormal's rounding is then 2^-39 of the bound for P scale, and 2^-25 of it,
+// with P's weight, for the scale.
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -57,6 +66,10 @@ namespace {
 constexpr int kWarpsW = 4;
 constexpr int kThreadsW = kWarpsW * 32;
 constexpr int kClusterRows = 4096;
+// 4-bit cache: log2 of P's factor; pairs of fp16: the least and the most a group's bound may be (2^-14, 2^14), and
+// what a pair of powers of two is taken from for their inverses (the exponents mirrored)
+constexpr float kLift = 14.f;
+constexpr uint32_t kBoundLeast = 0x04000400u, kBoundMost = 0x74007400u, kPow2Inverse = 0x78007800u;
 
 // rows a sequence may see at most (the lengths are on the device)
 long long win_decode_rows(const WinDecodeArgs& a) {
@@ -166,6 +179,20 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {  // (a NaN gives the other operand)
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmin2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// both halves of x in [-1, 1]
+__device__ __forceinline__ bool at_most_1(uint32_t x) {
+  return __hble2(__habs2(*reinterpret_cast<const __half2*>(&x)), __half2half2(__ushort_as_half(0x3c00)));
 }
 __device__ __forceinline__ float h_lo(uint32_t x) { return __low2float(*reinterpret_cast<const __half2*>(&x)); }
 __device__ __forceinline__ float h_hi(uint32_t x) { return __high2float(*reinterpret_cast<const __half2*>(&x)); }
@@ -453,6 +480,9 @@ __global__ void __launch_bounds__(kThreadsW, WSmem<INT4, D, NT, SPLIT>::REGS)
   float o[NT][D / 16][4];          // O^T: rows = channels, columns = heads 2c, 2c + 1
   float oz[NT][4];                 // 4-bit: sum of p * zero, row r = group r % NG (D = 128: rows 4 .. 7)
   float m[NT][2], l[NT][2];        // heads 2c, 2c + 1 (log2 domain; l: this lane's rows only)
+  uint32_t over[NG / 2];           // 4-bit: 1 over the bounds of the groups' value scales (pairs); o is in their units
+#pragma unroll
+  for (int i = 0; i < NG / 2; ++i) over[i] = kPow2Inverse - kBoundLeast;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -480,6 +510,19 @@ __global__ void __launch_bounds__(kThreadsW, WSmem<INT4, D, NT, SPLIT>::REGS)
     const uint32_t st = ring + stage * C::STAGE;
     const int rows = vis.n - (u * kWarpsW + warp) * CH;  // of this warp's share that exist
     if (rows > 0) {
+    // 4-bit: is a value scale of this lane's row (past the end: zeros) beyond its bound?  (Looked at before or after
+    // the scores, whichever the compiler fits better into 128 registers: before them 8 sequences of up to 131072 rows
+    // take 156 us, after them 162; 24 of 2048 to 4096, in clusters, 28.6 and 26.9.)
+    constexpr bool EARLY = SPLIT && D == 128;
+    const uint32_t va = st + C::OFF_VP + lane * C::PAR;
+    bool grow = false;
+    auto look = [&]() {
+      uint2 x = make_uint2(0u, 0u);
+      if constexpr (NG == 4) x = lds64(va);
+      else x.x = lds32(va);
+      grow = !at_most_1(hmul2(x.x, over[0])) || (NG == 4 && !at_most_1(hmul2(x.y, over[NG / 2 - 1])));
+    };
+    if constexpr (INT4 && EARLY) look();
     // scores of MT x 16 positions: rows r and r + 8
     float s[NT][MT][4];
     if constexpr (!INT4)
@@ -553,6 +596,16 @@ __global__ void __launch_bounds__(kThreadsW, WSmem<INT4, D, NT, SPLIT>::REGS)
           for (int j = 0; j < 4; ++j) s[t][mt][j] = fmaf(acc[t][j], 0x1p24f, s[t][mt][j]);
       }
     }
+    if constexpr (INT4 && !EARLY) look();
+    if (rows < CH) {  // the last rows: none past the end
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (mt * 16 + (j >> 1) * 8 + r >= rows) s[t][mt][j] = -INFINITY;
+    }
     // running maximum, probabilities (P^T as the B operand: rows of positions turned into columns)
     uint32_t pb[NT][MT][2];
 #pragma unroll
@@ -561,21 +614,19 @@ __global__ void __launch_bounds__(kThreadsW, WSmem<INT4, D, NT, SPLIT>::REGS)
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (rows < CH && mt * 16 + (j >> 1) * 8 + r >= rows) s[t][mt][j] = -INFINITY;
-          mx[j & 1] = fmaxf(mx[j & 1], s[t][mt][j]);
-        }
+        for (int j = 0; j < 4; ++j) mx[j & 1] = fmaxf(mx[j & 1], s[t][mt][j]);
       float f[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], off));
-        const float mn = fmaxf(m[t][j], mx[j] * sc[t][j]);
+        // (4-bit: rounded up, so that no P passes 2^kLift)
+        const float mn = fmaxf(m[t][j], INT4 ? __fmul_ru(mx[j], sc[t][j]) : mx[j] * sc[t][j]);
         f[j] = (mn == m[t][j]) ? 1.f : fast_exp2(m[t][j] - mn);
         m[t][j] = mn;
-        mx[j] = mn == -INFINITY ? 0.f : mn;
+        mx[j] = mn == -INFINITY ? 0.f : (INT4 ? __fadd_ru(mn, -kLift) : mn);
       }
-      if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+      if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f || (INT4 && t == 0 && grow))) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -584,6 +635,30 @@ __global__ void __launch_bounds__(kThreadsW, WSmem<INT4, D, NT, SPLIT>::REGS)
         for (int j = 0; j < 4; ++j) oz[t][j] *= f[j & 1];
         l[t][0] *= f[0];
         l[t][1] *= f[1];
+        if constexpr (INT4) {
+          if (t == 0 && __any_sync(0xffffffffu, grow)) {
+            // a scale is past its bound: the bounds raised, what is summed so far (all heads') in units of the new ones
+#pragma unroll
+            for (int k = 0; k < NG / 2; ++k) {
+              const uint32_t was = kPow2Inverse - over[k];
+              uint32_t up = hmax2(lds32(va + 4 * k) & 0x7fff7fffu, was);
+#pragma unroll
+              for (int off = 1; off < 32; off <<= 1) up = hmax2(up, __shfl_xor_sync(0xffffffffu, up, off));
+              up = hmin2((up + 0x03ff03ffu) & 0x7c007c00u, kBoundMost);  // to a power of two
+              over[k] = kPow2Inverse - up;
+              const float g0 = h_lo(was) * h_lo(over[k]), g1 = h_hi(was) * h_hi(over[k]);
+#pragma unroll
+              for (int tt = 0; tt < NT; ++tt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  o[tt][4 * k][j] *= g0;
+                  o[tt][4 * k + 1][j] *= g0;
+                  o[tt][4 * k + 2][j] *= g1;
+                  o[tt][4 * k + 3][j] *= g1;
+                }
+            }
+          }
+        }
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
@@ -613,7 +688,7 @@ __global__ void __launch_bounds__(kThreadsW, WSmem<INT4, D, NT, SPLIT>::REGS)
         // this lane's positions: 2c, 2c + 1 (first pair), 2c + 8, 2c + 9 (second); its
         // channels: 4r .. 4r + 3 of every group
         uint32_t x[2][NG];      // pair, group: nibbles of the pair's two positions
-        uint32_t sg[2][NG];     // the pair's scales of the group
+        uint32_t sg[2][NG];     // the pair's scales of the group, over their bound
         uint32_t zz[2];         // the pair's zeros of group r % NG (D = 128: in rows 4 .. 7)
         if constexpr (NG == 4) {
           // the parameter rows (scales, then zeros) of eight positions are an 8 x 8 matrix: transposed, rows 4 .. 7
@@ -631,7 +706,11 @@ __global__ void __launch_bounds__(kThreadsW, WSmem<INT4, D, NT, SPLIT>::REGS)
             x[pp][1] = __byte_perm(u0.x, u1.x, 0x7632);
             x[pp][2] = __byte_perm(u0.y, u1.y, 0x5410);
             x[pp][3] = __byte_perm(u0.y, u1.y, 0x7632);
-            const uint2 a0 = lds64(vpa), a1 = lds64(vpa + C::PAR);
+            uint2 a0 = lds64(vpa), a1 = lds64(vpa + C::PAR);
+            a0.x = hmul2(a0.x, over[0]);
+            a1.x = hmul2(a1.x, over[0]);
+            a0.y = hmul2(a0.y, over[NG / 2 - 1]);
+            a1.y = hmul2(a1.y, over[NG / 2 - 1]);
             sg[pp][0] = __byte_perm(a0.x, a1.x, 0x5410);
             sg[pp][1] = __byte_perm(a0.x, a1.x, 0x7632);
             sg[pp][2] = __byte_perm(a0.y, a1.y, 0x5410);
@@ -640,7 +719,9 @@ __global__ void __launch_bounds__(kThreadsW, WSmem<INT4, D, NT, SPLIT>::REGS)
             const uint32_t u0 = lds32(va0), u1 = lds32(va1);
             x[pp][0] = __byte_perm(u0, u1, 0x5410);
             x[pp][1] = __byte_perm(u0, u1, 0x7632);
-            const uint2 a0 = lds64(vpa), a1 = lds64(vpa + C::PAR);
+            uint2 a0 = lds64(vpa), a1 = lds64(vpa + C::PAR);
+            a0.x = hmul2(a0.x, over[0]);
+            a1.x = hmul2(a1.x, over[0]);
             sg[pp][0] = __byte_perm(a0.x, a1.x, 0x5410);
             sg[pp][1] = __byte_perm(a0.x, a1.x, 0x7632);
             zz[pp] = __byte_perm(a0.y, a1.y, (r & 1) ? 0x7632 : 0x5410);
@@ -710,9 +791,11 @@ __global__ void __launch_bounds__(kThreadsW, WSmem<INT4, D, NT, SPLIT>::REGS)
           for (int j = 0; j < 2; ++j) {
             // the lanes of accumulator row gg (D = 128: 4 + gg) hold the zeros' share of group gg for the same heads
             const float z = __shfl_sync(0xffffffffu, oz[t][j], 4 * (gg + (NG == 4 ? 4 : 0)) + c);
+            const uint32_t bound = kPow2Inverse - over[gg / 2];
+            const float u = (gg & 1) ? h_hi(bound) : h_lo(bound), u0 = u * 0x1p24f, u1 = u * 0x1p20f;
             *reinterpret_cast<float4*>(&mine.o[t * 8 + 2 * c + j][gg * 32 + r * 4]) =
-                make_float4(fmaf(o[t][2 * gg][j], 0x1p24f, z), fmaf(o[t][2 * gg][2 + j], 0x1p20f, z),
-                            fmaf(o[t][2 * gg + 1][j], 0x1p24f, z), fmaf(o[t][2 * gg + 1][2 + j], 0x1p20f, z));
+                make_float4(fmaf(o[t][2 * gg][j], u0, z), fmaf(o[t][2 * gg][2 + j], u1, z),
+                            fmaf(o[t][2 * gg + 1][j], u0, z), fmaf(o[t][2 * gg + 1][2 + j], u1, z));
           }
       }
     }
