@@ -78,6 +78,7 @@ struct FCfg {
   // D = 64 leaves room for dQ by itself: two tiles of TMEM columns and two
   // staging tiles (at D = 128 it takes dP's columns, and the dS and dO spaces)
   static constexpr bool APART = D == 64;
+  static constexpr int NDQ = APART ? 2 : 1;  // dQ tiles in TMEM, by step (1 or 2)
   static constexpr int OFF_STG = OFF_DS + DS_BYTES;
   static constexpr int STG_BYTES = APART ? kRows * D * 4 : 0;
   static constexpr int OFF_VEC = OFF_STG + 2 * STG_BYTES;  // stage s: lse[128] then delta[128] (fp32)
@@ -94,8 +95,8 @@ struct FCfg {
   static constexpr int T_DP = 128;
   static constexpr int T_DV = 256;
   static constexpr int T_DK = 256 + D;
-  static constexpr int T_DQ = APART ? T_DK + D : T_DP;  // APART: of step j at T_DQ + (j & 1) * D
-  static_assert(T_DK + D + (APART ? 2 * D : 0) <= 512, "TMEM budget");
+  static constexpr int T_DQ = APART ? T_DK + D : T_DP;  // of step j at T_DQ + (j % NDQ) * D
+  static_assert(T_DK + D + (APART ? NDQ * D : 0) <= 512, "TMEM budget");
 };
 
 // what the producer publishes with each Q stage: the query tile's first
@@ -108,9 +109,12 @@ struct StepInfo {
 struct FBars {
   uint64_t k_full, k_empty, v_full, v_empty;
   uint64_t q_full[2], q_empty[2], do_full[2], do_empty[2];
-  uint64_t s_full, p_full, dp_full, dst_full, dss_full, dq_full, dq_free, staged, staged_ds, ds_free;
+  uint64_t s_full, p_full, dp_full, dst_full, dss_full, dq_free, staged, staged_ds, ds_free;
   uint64_t dv_full, dk_full, done;
-  uint64_t dq_free2[2], staged2[2], stg_empty[2];  // APART: per buffer
+  // per dQ tile.  (One dq_full for both of APART's tiles would not do: two of them may be formed before the read-out
+  // looks for the first, and the barrier, two phases on, would show it the parity of a phase that is not complete.)
+  uint64_t dq_full[2];
+  uint64_t dq_free2[2], staged2[2], stg_empty[2];  // APART
   uint64_t clc, unit_full[2], unit_empty[2];  // the next unit's number has come; units published, read
 };
 static_assert(sizeof(FBars) <= 320, "barrier area");
@@ -242,7 +246,6 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_bwd_window_kernel(const __g
     mbar_init(&bar.dp_full, 1);
     mbar_init(&bar.dst_full, 256);
     mbar_init(&bar.dss_full, 256);
-    mbar_init(&bar.dq_full, 1);
     mbar_init(&bar.dq_free, 128);
     mbar_init(&bar.staged, 128);
     mbar_init(&bar.staged_ds, 128);
@@ -252,6 +255,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_bwd_window_kernel(const __g
     mbar_init(&bar.done, 1);
     mbar_init(&bar.clc, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.dq_full[i], 1);
       mbar_init(&bar.dq_free2[i], 128);
       mbar_init(&bar.staged2[i], 128);
       mbar_init(&bar.stg_empty[i], 1);
@@ -282,6 +286,8 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_bwd_window_kernel(const __g
     if (lane == 0) mbar_arrive(&bar.unit_empty[r & 1]);
     return (bool)__all_sync(0xffffffffu, u.b >= 0);
   };
+  // dQ of step j is formed (or the wait failed)
+  auto await_dq = [&](int j) { return mbar_wait(&bar.dq_full[j & (C::NDQ - 1)], (j >> (C::NDQ - 1)) & 1, ab); };
   auto unit_of_thread = [&](int r, BwdUnit& u) {
     if (!mbar_wait(&bar.unit_full[r & 1], (r >> 1) & 1, ab)) return false;
     u = us[r & 1];
@@ -317,7 +323,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_bwd_window_kernel(const __g
       Steps it;
       it.begin(wt, a.win, u, G, a.parts);
       do {
-        mbar_wait(&bar.dq_full, gs & 1, ab);  // runs on after an abort: the staging is garbage, the waits bounded
+        await_dq(gs);  // runs on after an abort: the staging is garbage, the waits bounded
         tc_fence_after();
         uint32_t o[2][32];
         if constexpr (C::APART) {
@@ -544,7 +550,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_bwd_window_kernel(const __g
         for (int kk = 0; kk < kRows / 16; ++kk)
           mma_ss(tm + C::T_DQ + buf * D, dS_mn + ((kk * 16 * 128) >> 4), dK_mn + ((kk * 16 * 128) >> 4), IDESC_DQ,
                  kk > 0 ? 1u : 0u);
-        mma_commit(&bar.dq_full);
+        mma_commit(&bar.dq_full[buf]);
         }
       };
 
@@ -724,7 +730,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_bwd_window_kernel(const __g
         tc_fence_before();
         mbar_arrive(&bar.dst_full);
         // the dS space is free: the last dQ is formed (APART), or its tile has left the space too
-        if (gs > 0) mbar_wait(C::APART ? &bar.dq_full : &bar.ds_free, (gs - 1) & 1, ab);
+        if (gs > 0) C::APART ? await_dq(gs - 1) : mbar_wait(&bar.ds_free, (gs - 1) & 1, ab);
         unsigned char* dsr = smem + C::OFF_DS + g * (kRows * 128) + row * 128;  // this key row of query half g
 #pragma unroll
         for (int chunk = 0; chunk < 8; ++chunk)  // 8 query columns per 16-byte chunk

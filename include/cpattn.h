@@ -361,7 +361,8 @@ int kv_read_int4(const void* kcodes, const void* kparams, const void* vcodes, co
  * exactly; scales and zeros are applied in fp32 to the scores.  For the values
  * the probabilities are rounded to fp16, and again times each group's scale,
  * 2^-11 of themselves each time, whatever the size of the values: probability
- * times scale down to 2^-28 of the group's largest, scales down to 2^-14 of it.
+ * times scale down to 2^-28 of the group's largest (or 2^-14, if that is more),
+ * scales down to 2^-14 of it.
  * q and out [B, Hq, D] bf16; the rest as gqa_decode_window.
  */
 int gqa_decode_int4(const void* q, const void* kcodes, const void* kparams, const void* vcodes, const void* vparams,
