@@ -199,6 +199,19 @@ struct ProfScope {  // brackets one kernel launch when profiling is on
   cudaStream_t stream = nullptr;
 };
 
+// Host memory to the device, and device memory cleared, for good: a copy from
+// pageable memory and a memset may return before the device has them, and a
+// stream that does not wait for the legacy one (PyTorch's own streams, say) could
+// launch a kernel that reads what was there before.
+cudaError_t copy_to_device(void* dst, const void* src, size_t bytes) {
+  const cudaError_t e = cudaMemcpy(dst, src, bytes, cudaMemcpyHostToDevice);
+  return e != cudaSuccess ? e : cudaStreamSynchronize(cudaStreamLegacy);
+}
+cudaError_t clear_device(void* dst, size_t bytes) {
+  const cudaError_t e = cudaMemset(dst, 0, bytes);
+  return e != cudaSuccess ? e : cudaStreamSynchronize(cudaStreamLegacy);
+}
+
 int get_state(DevState** out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -210,8 +223,12 @@ int get_state(DevState** out) {
     cudaDeviceGetAttribute(&s.cc_minor, cudaDevAttrComputeCapabilityMinor, dev);
     e = cudaMalloc(&s.err, sizeof(int));
     if (e != cudaSuccess) { s.err = nullptr; return fail(CPATTN_ERR_NO_MEMORY, "cudaMalloc(error word) failed"); }
-    e = cudaMemset(s.err, 0, sizeof(int));
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMemset");
+    e = clear_device(s.err, sizeof(int));
+    if (e != cudaSuccess) {
+      cudaFree(s.err);
+      s.err = nullptr;
+      return cuda_fail(e, "cudaMemset");
+    }
   }
   *out = &s;
   return CPATTN_OK;
@@ -251,7 +268,7 @@ int upload(DevBuf<T>& b, const std::vector<T>& v) {
   cudaError_t e = cudaMalloc(&b.ptr, std::max<size_t>(1, v.size()) * sizeof(T));
   if (e != cudaSuccess) { b.ptr = nullptr; return fail(CPATTN_ERR_NO_MEMORY, "cudaMalloc(work list) failed"); }
   if (!v.empty()) {
-    e = cudaMemcpy(b.ptr, v.data(), v.size() * sizeof(T), cudaMemcpyHostToDevice);
+    e = copy_to_device(b.ptr, v.data(), v.size() * sizeof(T));
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpy(work list)");
   }
   b.n = v.size();
@@ -1588,7 +1605,7 @@ int cp_attn_check_device(cudaStream_t stream) {
   if (it != g_dev.end() && it->second.err) {
     e = cudaMemcpy(&word, it->second.err, sizeof(int), cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpy(error word)");
-    if (word != DEV_OK) cudaMemset(it->second.err, 0, sizeof(int));
+    if (word != DEV_OK && (e = clear_device(it->second.err, sizeof(int))) != cudaSuccess) return cuda_fail(e, "cudaMemset");
   }
   int word_na = 0;  // the allocation-free decode keeps its own word in its static array
   e = noalloc_take_error(&word_na);
