@@ -648,10 +648,12 @@ __device__ __forceinline__ void clc_ask(void* answer, uint64_t* bar) {
                "r"(smem_u32(bar))
                : "memory");
 }
-// the number of the CTA struck off, -1 if none was left
+// the number of the CTA struck off, -1 if none was left.  (The fence puts this
+// read before the next answer, which the async proxy writes to the same bytes.)
 __device__ __forceinline__ int clc_answer(const void* answer) {
   const volatile unsigned long long* w = static_cast<const volatile unsigned long long*>(answer);
   const unsigned long long lo = w[0], hi = w[1];
+  fence_proxy_async_smem();
   uint32_t got, x;
   asm volatile(
       "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\tmov.b128 h, {%2, %3};\n\t"
