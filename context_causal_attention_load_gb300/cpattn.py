@@ -434,6 +434,8 @@ def _workspace(query, dev, shape, like):
     if n is None:  # (a function of the shape and the device alone)
         c = ctypes.c_size_t(0)
         _run(query, dev, *shape, ctypes.byref(c))
+        if len(_ws_bytes) >= 4096:  # (a program may call with any number of shapes)
+            _ws_bytes.clear()
         n = _ws_bytes[query, dev, shape] = c.value
     return (torch.empty(n, dtype=torch.uint8, device=like.device) if n else None), n
 

@@ -138,11 +138,64 @@ struct UnitPlan {
   int ncta = 0;
 };
 
-// the windowed backward's: units, the parts of split units, the tiles to join
+// windowed attention's work lists.  The backward's: units, the parts of split units, the tiles to join
+template <typename T>
+size_t kept(const DevBuf<T>& b) {  // device bytes it takes
+  return (b.n * sizeof(T) + 511) / 512 * 512;
+}
+struct WinFwdPlan {
+  DevBuf<FwdUnit> units;
+  size_t bytes() const { return kept(units); }
+  void release() { cudaFree(units.ptr); }
+};
 struct WinBwdPlan {
   DevBuf<BwdUnit> units;
   DevBuf<WinPart> parts;
   DevBuf<WinJoin> joins;
+  size_t bytes() const { return kept(units) + kept(parts) + kept(joins); }
+  void release() {
+    cudaFree(units.ptr);
+    cudaFree(parts.ptr);
+    cudaFree(joins.ptr);
+  }
+};
+
+// Work lists by shape, window and sinks.  A program may call with any number of
+// lengths: past kPlanBytes the lists least recently used go, down to half of it.
+// One that was used in a stream capture stays: the graph holds its address.
+constexpr size_t kPlanBytes = 16 << 20;
+template <typename Plan>
+struct PlanCache {
+  struct Entry {
+    Plan plan;
+    unsigned long long used = 0;
+    bool held = false;  // by a graph
+  };
+  std::map<std::vector<int>, Entry> at;
+  size_t bytes = 0;  // of the lists that may go
+  unsigned long long calls = 0;
+
+  void make_room(size_t more) {
+    if (bytes + more <= kPlanBytes || bytes == 0) return;
+    if (cudaDeviceSynchronize() != cudaSuccess) {  // (kernels in flight may read them)
+      cudaGetLastError();
+      return;
+    }
+    std::vector<std::pair<unsigned long long, const std::vector<int>*>> order;
+    for (const auto& x : at)
+      if (!x.second.held) order.push_back({x.second.used, &x.first});
+    std::sort(order.begin(), order.end());
+    for (const auto& o : order) {
+      if (bytes + more <= kPlanBytes / 2) break;
+      auto it = at.find(*o.second);
+      bytes -= it->second.plan.bytes();
+      it->second.plan.release();
+      at.erase(it);
+    }
+  }
+  void release() {
+    for (auto& x : at) x.second.plan.release();
+  }
 };
 
 struct DevState {
@@ -151,8 +204,8 @@ struct DevState {
   int* err = nullptr;  // device error word
   std::map<std::vector<int>, UnitPlan<FwdUnit>> fwd_units;
   std::map<std::vector<int>, UnitPlan<BwdUnit>> bwd_units;
-  std::map<std::vector<int>, DevBuf<FwdUnit>> win_fwd;  // windowed attention: keyed by shape, window and sinks
-  std::map<std::vector<int>, WinBwdPlan> win_bwd;
+  PlanCache<WinFwdPlan> win_fwd;
+  PlanCache<WinBwdPlan> win_bwd;
   DevBuf<float> bwd_stats;  // lse_l2 then delta
   DevBuf<float> dq_acc;     // fused backward's fp32 dQ accumulator
   DevBuf<float> rope_acc;   // MLA with shared rope keys: dK's rope columns summed over heads
@@ -630,16 +683,20 @@ int check_window(int window, int sinks) {
   return CPATTN_OK;
 }
 
+bool capturing(cudaStream_t st) {
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return cap != cudaStreamCaptureStatusNone;
+}
+
 // A call that has to allocate (the state of a device, a work list) cannot do
 // so while its stream is being captured: refused before anything is touched,
 // so that the capture stays valid.
 int not_capturing(cudaStream_t st, const char* what) {
-  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) {
-    cudaGetLastError();
-    return CPATTN_OK;
-  }
-  if (cap != cudaStreamCaptureStatusNone)
+  if (capturing(st))
     return fail(CPATTN_ERR_INVALID_ARG, "the first call %s allocates: make it before the stream capture", what);
   return CPATTN_OK;
 }
@@ -698,21 +755,42 @@ std::vector<std::pair<long long, FwdUnit>> build_win_fwd(const AttnShape& sh, co
   return w;
 }
 
-int win_fwd_cached(DevState& ds, const AttnShape& sh, const Window& win, cudaStream_t st, DevBuf<FwdUnit>** out) {
-  std::vector<int> key{sh.B, sh.Hq, sh.Hkv, sh.S, sh.cp, sh.lb, win.window, win.sinks};
-  auto it = ds.win_fwd.find(key);
-  if (it == ds.win_fwd.end()) {
+// the work list of a key, from `build` if there is none
+template <typename Plan, typename Build>
+int plan_cached(PlanCache<Plan>& c, const AttnShape& sh, const Window& win, cudaStream_t st, Plan** out, Build build) {
+  using Entry = typename PlanCache<Plan>::Entry;
+  const std::vector<int> key{sh.B, sh.Hq, sh.Hkv, sh.S, sh.cp, sh.lb, win.window, win.sinks};
+  auto it = c.at.find(key);
+  if (it == c.at.end()) {
     int rc = not_capturing(st, "of a shape");
     if (rc) return rc;
-    DevBuf<FwdUnit> list;
-    if ((rc = upload(list, longest_first(build_win_fwd(sh, win))))) {
-      cudaFree(list.ptr);
-      return rc;
-    }
-    it = ds.win_fwd.emplace(key, list).first;
+    Entry fresh;
+    struct Undo {
+      Plan* plan;
+      ~Undo() {
+        if (plan) plan->release();
+      }
+    } undo{&fresh.plan};
+    if ((rc = build(fresh.plan))) return rc;
+    const size_t more = fresh.plan.bytes();
+    c.make_room(more);
+    it = c.at.emplace(key, fresh).first;
+    undo.plan = nullptr;
+    c.bytes += more;
   }
-  *out = &it->second;
+  Entry& e = it->second;
+  e.used = ++c.calls;
+  if (!e.held && capturing(st)) {
+    e.held = true;
+    c.bytes -= e.plan.bytes();
+  }
+  *out = &e.plan;
   return CPATTN_OK;
+}
+
+int win_fwd_cached(DevState& ds, const AttnShape& sh, const Window& win, cudaStream_t st, WinFwdPlan** out) {
+  return plan_cached(ds.win_fwd, sh, win, st, out,
+                     [&](WinFwdPlan& p) { return upload(p.units, longest_first(build_win_fwd(sh, win))); });
 }
 
 // The steps a unit may have at most before it comes in equal parts: of an even
@@ -809,27 +887,16 @@ void build_win_bwd(const AttnShape& sh, const Window& win, int num_sms, std::vec
 }
 
 int win_bwd_cached(DevState& ds, const AttnShape& sh, const Window& win, cudaStream_t st, WinBwdPlan** out) {
-  std::vector<int> key{sh.B, sh.Hq, sh.Hkv, sh.S, sh.cp, sh.lb, win.window, win.sinks};
-  auto it = ds.win_bwd.find(key);
-  if (it == ds.win_bwd.end()) {
-    int rc = not_capturing(st, "of a shape");
-    if (rc) return rc;
+  return plan_cached(ds.win_bwd, sh, win, st, out, [&](WinBwdPlan& p) {
     std::vector<std::pair<long long, BwdUnit>> w;
     std::vector<WinPart> parts;
     std::vector<WinJoin> joins;
     build_win_bwd(sh, win, ds.num_sms, w, parts, joins);
-    WinBwdPlan plan;
-    if ((rc = upload(plan.units, longest_first(std::move(w)))) || (rc = upload(plan.parts, parts)) ||
-        (rc = upload(plan.joins, joins))) {
-      cudaFree(plan.units.ptr);
-      cudaFree(plan.parts.ptr);
-      cudaFree(plan.joins.ptr);
-      return rc;
-    }
-    it = ds.win_bwd.emplace(key, plan).first;
-  }
-  *out = &it->second;
-  return CPATTN_OK;
+    int rc = upload(p.units, longest_first(std::move(w)));
+    if (!rc) rc = upload(p.parts, parts);
+    if (!rc) rc = upload(p.joins, joins);
+    return rc;
+  });
 }
 
 // the windowed backward's workspace: byte offsets of its pieces
@@ -1369,8 +1436,8 @@ int cp_attn_fwd_window(const void* q, const void* k, const void* v, void* out, f
     std::lock_guard<std::mutex> lk(g_mu);
     DevState* ds;
     if ((rc = get_state_for(stream, &ds))) return rc;
-    DevBuf<FwdUnit>* units;
-    if ((rc = win_fwd_cached(*ds, sh, a.win, stream, &units))) return rc;
+    WinFwdPlan* plan;
+    if ((rc = win_fwd_cached(*ds, sh, a.win, stream, &plan))) return rc;
     if ((rc = make_tmap(&a.tq, q, B, S, Hq, D, 128))) return rc;
     if ((rc = make_tmap(&a.tk, k, B, S, Hkv, D, 128))) return rc;
     if ((rc = make_tmap(&a.tv, v, B, S, Hkv, D, 128))) return rc;
@@ -1379,8 +1446,8 @@ int cp_attn_fwd_window(const void* q, const void* k, const void* v, void* out, f
     if ((rc = make_tmap(&a.tvs, v, B, S, Hkv, D, kWinNarrow))) return rc;
     a.out = out;
     a.lse = lse;
-    a.units = units->ptr;
-    a.n_units = (int)units->n;
+    a.units = plan->units.ptr;
+    a.n_units = (int)plan->units.n;
     a.sh = sh;
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
     a.err = ds->err;
@@ -1674,12 +1741,8 @@ int cp_attn_release(void) {
   DevState& s = it->second;
   for (auto& kv : s.fwd_units) { cudaFree(kv.second.units.ptr); cudaFree(kv.second.off.ptr); }
   for (auto& kv : s.bwd_units) { cudaFree(kv.second.units.ptr); cudaFree(kv.second.off.ptr); }
-  for (auto& kv : s.win_fwd) cudaFree(kv.second.ptr);
-  for (auto& kv : s.win_bwd) {
-    cudaFree(kv.second.units.ptr);
-    cudaFree(kv.second.parts.ptr);
-    cudaFree(kv.second.joins.ptr);
-  }
+  s.win_fwd.release();
+  s.win_bwd.release();
   cudaFree(s.bwd_stats.ptr);
   cudaFree(s.dq_acc.ptr);
   cudaFree(s.rope_acc.ptr);

@@ -270,7 +270,11 @@ int gqa_decode_noalloc(const void* q, const void* kcache, const void* vcache, co
  * shared.  The first call on a device, and the first windowed forward or
  * backward of a shape, allocate: made while the stream is being captured
  * they are refused with CPATTN_ERR_INVALID_ARG and the capture stays valid.
- * cp_attn_release frees the work lists: captured graphs must be gone by then.
+ * Work lists of up to 16 MB are kept per device and direction (a list takes 32
+ * bytes per two tiles of 128 queries, or 16 per key tile and KV head); past
+ * that the device is waited for and the shapes least recently called go, whose
+ * next call is a first one again.  What a captured call uses stays until
+ * cp_attn_release, which frees all lists: captured graphs must be gone by then.
  */
 
 /*
