@@ -198,11 +198,12 @@ __global__ void __launch_bounds__(kThreadsKv, 4) kv_append_int4_kernel(const __g
           else w[0] = v;
         }
       } else if (min(near & 0xffffu, near >> 16) <= 6u) {
-        // the pairs that come close to a tie, exactly: x - zero against (k + 1/2) scale
+        // the pairs that come close to a tie, exactly: x - zero against (k + 1/2) scale.  (The other of a pair may lie
+        // below zero, which is rounded where the least value is small: k is -1 then.)
         auto code = [&](float v) {
           const float d = v - z, k = floorf(d * inv), t = fmaf(-(k + 0.5f), s, d);
-          const uint32_t n = (uint32_t)k;
-          return n + (t > 0.f || (t == 0.f && (n & 1)) ? 1u : 0u);
+          const int n = (int)k;
+          return (uint32_t)(n + (t > 0.f || (t == 0.f && (n & 1)) ? 1 : 0));
         };
 #pragma unroll
         for (int q = 0; q < 2; ++q)
