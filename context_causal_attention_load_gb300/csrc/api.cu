@@ -685,9 +685,10 @@ int check_window(int window, int sinks) {
 
 bool capturing(cudaStream_t st) {
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) {
+  const cudaError_t e = cudaStreamIsCapturing(st, &cap);
+  if (e != cudaSuccess) {
     cudaGetLastError();
-    return false;
+    return e == cudaErrorStreamCaptureImplicit;  // (the legacy stream, while one that waits for it is captured)
   }
   return cap != cudaStreamCaptureStatusNone;
 }
