@@ -445,8 +445,8 @@ _ws_bytes = {}
 
 
 def _count(n):
-    """A window or a number of sinks as a C int: all that passes one is everything."""
-    return min(int(n), 2 ** 31 - 1)
+    """A window or a number of sinks as a C int: all that passes one is everything, all below zero refused."""
+    return max(-1, min(int(n), 2 ** 31 - 1))
 
 
 def attn_fwd_window(q, k, v, cp, window, sinks=0, load_balance=True, out=None, lse=None):
