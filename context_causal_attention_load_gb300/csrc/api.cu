@@ -1535,7 +1535,7 @@ int cp_attn_bwd_window(const void* q, const void* k, const void* v, const void* 
     if (e != cudaSuccess) return cuda_fail(e, "attn_bwd_window launch");
     {
       ProfScope ps("bwd_dq_round", stream);
-      e = launch_bwd_window_finish(a, plan->joins.ptr, (int)plan->joins.n, stream);
+      e = launch_bwd_window_finish(a, plan->joins.ptr, (int)plan->joins.n, ds->num_sms, stream);
     }
     if (e != cudaSuccess) return cuda_fail(e, "dq rounding launch");
     return CPATTN_OK;

@@ -941,9 +941,9 @@ cudaError_t launch_attn_bwd_window(const BwdArgs& a, cudaStream_t st) {
   return a.sh.Dqk == 64 ? launch_t<64>(a, st) : launch_t<128>(a, st);
 }
 
-cudaError_t launch_bwd_window_finish(const BwdArgs& a, const WinJoin* joins, int n_joins, cudaStream_t st) {
+cudaError_t launch_bwd_window_finish(const BwdArgs& a, const WinJoin* joins, int n_joins, int num_sms, cudaStream_t st) {
   const long long n8 = (long long)a.sh.B * a.sh.S * a.sh.Hq * a.sh.Dqk / 8;
-  const long long want = (n8 + 255) / 256, most = 152LL * 16;
+  const long long want = (n8 + 255) / 256, most = 16LL * num_sms;
   const int blocks_dq = (int)(want < most ? want : most);
   return launch_overlapped(a.sh.Dqk == 64 ? bwd_window_finish_kernel<64> : bwd_window_finish_kernel<128>,
                            dim3(blocks_dq + 8 * n_joins), 256, 0, st, a, joins, n8, blocks_dq);

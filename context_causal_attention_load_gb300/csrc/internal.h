@@ -199,7 +199,7 @@ cudaError_t launch_attn_bwd_fused(const BwdArgs& a, int grid, cudaStream_t st);
 cudaError_t launch_bwd_window_prepare(const void* out, const void* dout, const float* lse, const BwdArgs& a,
                                       cudaStream_t st);
 cudaError_t launch_attn_bwd_window(const BwdArgs& a, cudaStream_t st);
-cudaError_t launch_bwd_window_finish(const BwdArgs& a, const WinJoin* joins, int n_joins, cudaStream_t st);
+cudaError_t launch_bwd_window_finish(const BwdArgs& a, const WinJoin* joins, int n_joins, int num_sms, cudaStream_t st);
 cudaError_t launch_bwd_dq_round(const float* acc, void* dq, long long n, float scale, cudaStream_t st);
 // natural-order tensors (zero-copy load balance): the accumulator is in slot order
 cudaError_t launch_bwd_dq_round_nat(const float* acc, void* dq, const AttnShape& sh, float scale, cudaStream_t st);
