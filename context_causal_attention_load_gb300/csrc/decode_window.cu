@@ -69,6 +69,9 @@ constexpr int kClusterRows = 4096;
 // 4-bit cache: log2 of P's factor; pairs of fp16: the least and the most a group's bound may be (2^-14, 2^14), and
 // what a pair of powers of two is taken from for their inverses (the exponents mirrored)
 constexpr float kLift = 14.f;
+// units of a warp after which the zeros' sums join the codes' (8 sequences of up to 131072 rows, flat scores: error
+// 0.0024 -> 0.0017, of which 0.0016 is the result's rounding, 156 -> 161 us; after 4 or 8 units no less)
+constexpr int kFold = 16;
 constexpr uint32_t kBoundLeast = 0x04000400u, kBoundMost = 0x74007400u, kPow2Inverse = 0x78007800u;
 
 // rows a sequence may see at most (the lengths are on the device)
@@ -501,6 +504,8 @@ __global__ void __launch_bounds__(kThreadsW, WSmem<INT4, D, NT, SPLIT>::REGS)
   const uint32_t vo1 =
       C::OFF_V + (NG == 4 ? off4<C::ROW>(2 * c + 1, r >> 1) + (r & 1) * 8 : off4<C::ROW>(2 * c + 1, r >> 2) + (r & 3) * 4);
   const uint32_t vpo = C::OFF_VP + 2 * c * C::PAR;
+  // the lanes of accumulator row gg (D = 128: 4 + gg) hold the zeros' share of group gg for the same heads
+  auto zeros_of = [&](float x, int gg) { return __shfl_sync(0xffffffffu, x, 4 * (gg + (NG == 4 ? 4 : 0)) + c); };
   for (int i = 0; i < seg; ++i) {
     const int u = ur + i * ustep;
     if (i + 1 < seg) load(u + ustep, stage ^ 1);
@@ -510,19 +515,15 @@ __global__ void __launch_bounds__(kThreadsW, WSmem<INT4, D, NT, SPLIT>::REGS)
     const uint32_t st = ring + stage * C::STAGE;
     const int rows = vis.n - (u * kWarpsW + warp) * CH;  // of this warp's share that exist
     if (rows > 0) {
-    // 4-bit: is a value scale of this lane's row (past the end: zeros) beyond its bound?  (Looked at before or after
-    // the scores, whichever the compiler fits better into 128 registers: before them 8 sequences of up to 131072 rows
-    // take 156 us, after them 162; 24 of 2048 to 4096, in clusters, 28.6 and 26.9.)
-    constexpr bool EARLY = SPLIT && D == 128;
+    // 4-bit: is a value scale of this lane's row (past the end: zeros) beyond its bound?
     const uint32_t va = st + C::OFF_VP + lane * C::PAR;
     bool grow = false;
-    auto look = [&]() {
+    if constexpr (INT4) {
       uint2 x = make_uint2(0u, 0u);
       if constexpr (NG == 4) x = lds64(va);
       else x.x = lds32(va);
       grow = !at_most_1(hmul2(x.x, over[0])) || (NG == 4 && !at_most_1(hmul2(x.y, over[NG / 2 - 1])));
-    };
-    if constexpr (INT4 && EARLY) look();
+    }
     // scores of MT x 16 positions: rows r and r + 8
     float s[NT][MT][4];
     if constexpr (!INT4)
@@ -596,7 +597,6 @@ __global__ void __launch_bounds__(kThreadsW, WSmem<INT4, D, NT, SPLIT>::REGS)
           for (int j = 0; j < 4; ++j) s[t][mt][j] = fmaf(acc[t][j], 0x1p24f, s[t][mt][j]);
       }
     }
-    if constexpr (INT4 && !EARLY) look();
     if (rows < CH) {  // the last rows: none past the end
 #pragma unroll
       for (int t = 0; t < NT; ++t)
@@ -626,7 +626,8 @@ __global__ void __launch_bounds__(kThreadsW, WSmem<INT4, D, NT, SPLIT>::REGS)
         m[t][j] = mn;
         mx[j] = mn == -INFINITY ? 0.f : (INT4 ? __fadd_ru(mn, -kLift) : mn);
       }
-      if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f || (INT4 && t == 0 && grow))) {
+      const bool fold = INT4 && i % kFold == kFold - 1;
+      if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f || (INT4 && t == 0 && grow) || fold)) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -636,6 +637,23 @@ __global__ void __launch_bounds__(kThreadsW, WSmem<INT4, D, NT, SPLIT>::REGS)
         l[t][0] *= f[0];
         l[t][1] *= f[1];
         if constexpr (INT4) {
+          // (A flat cache's two sums grow with the rows and cancel; the matrix instruction rounds each time by what it
+          // adds to.  So now and then the zeros' sums go where the codes' are.)
+          if (fold) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+              for (int gg = 0; gg < NG; ++gg) {
+                const float z = zeros_of(oz[t][j], gg);
+                const float g = ((gg & 1) ? h_hi(over[gg / 2]) : h_lo(over[gg / 2])) * 0x1p-24f;
+                o[t][2 * gg][j] = fmaf(z, g, o[t][2 * gg][j]);
+                o[t][2 * gg][2 + j] = fmaf(z, g * 16.f, o[t][2 * gg][2 + j]);
+                o[t][2 * gg + 1][j] = fmaf(z, g, o[t][2 * gg + 1][j]);
+                o[t][2 * gg + 1][2 + j] = fmaf(z, g * 16.f, o[t][2 * gg + 1][2 + j]);
+              }
+              oz[t][j] = 0.f;
+            }
+          }
           if (t == 0 && __any_sync(0xffffffffu, grow)) {
             // a scale is past its bound: the bounds raised, what is summed so far (all heads') in units of the new ones
 #pragma unroll
@@ -789,8 +807,7 @@ __global__ void __launch_bounds__(kThreadsW, WSmem<INT4, D, NT, SPLIT>::REGS)
         for (int gg = 0; gg < NG; ++gg)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            // the lanes of accumulator row gg (D = 128: 4 + gg) hold the zeros' share of group gg for the same heads
-            const float z = __shfl_sync(0xffffffffu, oz[t][j], 4 * (gg + (NG == 4 ? 4 : 0)) + c);
+            const float z = zeros_of(oz[t][j], gg);
             const uint32_t bound = kPow2Inverse - over[gg / 2];
             const float u = (gg & 1) ? h_hi(bound) : h_lo(bound), u0 = u * 0x1p24f, u1 = u * 0x1p20f;
             *reinterpret_cast<float4*>(&mine.o[t * 8 + 2 * c + j][gg * 32 + r * 4]) =

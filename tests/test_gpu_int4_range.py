@@ -230,3 +230,37 @@ def test_a_group_that_is_not_a_number(Smax, which):
     bad[0, 2:, 64:96] = True
     assert np.isnan(got[bad]).all()
     assert (np.abs(got - terms[0]) <= _tolerance(terms, D))[~bad].all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_flat_caches(D):
+    """hundreds of rows a warp, weights alike: the sums of codes and of zeros grow with the rows and cancel.  Rounding
+    the exact result to bf16 alone gives an error r; P's and P * scale's rounding to fp16 add some 2^-11 * 0.6 *
+    sqrt(1 + (8.7 / 3.7)^2) = 0.0007 to it in quadrature (root mean squares of a uniform rounding, of a code and of a
+    value in scales), 9% of r = 0.0016; what adding in fp32 costs has to stay within the same again"""
+    B, Hkv, G, Smax = 6, 8, 2, 131072
+    g = torch.Generator(device="cuda").manual_seed(13)
+    cache = cp_.int4_cache(B, Hkv, Smax, D)
+    start = torch.zeros(B, dtype=torch.int32, device="cuda")
+    for t0 in range(0, Smax, 32768):
+        k, v = (torch.randn(B, 32768, Hkv, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+        cp_.kv_append_int4(k, v, start + t0, *cache)
+    del k, v
+    q = torch.randn(B, Hkv * G, D, generator=g, device="cuda").bfloat16()
+    lens = torch.full((B,), Smax, dtype=torch.int32, device="cuda")
+    got = cp_.gqa_decode_int4(q, *cache, lens)
+    cp_.check_device()
+    order = torch.tensor([W._nibble(D, ch) for ch in range(D)], device="cuda")
+
+    def values(codes, params):
+        n = torch.stack([codes & 15, codes >> 4], -1).flatten(-2)[..., order].double().unflatten(-1, (D // 32, 32))
+        return (n * params[..., 0, :].double()[..., None] + params[..., 1, :].double()[..., None]).flatten(-2)
+
+    want = torch.empty(q.shape, dtype=torch.float64, device="cuda")
+    for b in range(B):
+        for h in range(Hkv):
+            kk, vv = values(cache[0][b, h], cache[1][b, h]), values(cache[2][b, h], cache[3][b, h])
+            w = torch.softmax(q[b, h * G:(h + 1) * G].double() @ kk.T / D ** 0.5, -1)
+            want[b, h * G:(h + 1) * G] = w @ vv
+    err, r = (got.double() - want).norm(), (want.bfloat16().double() - want).norm()
+    assert err <= 1.18 * r, float(err / r)
