@@ -29,7 +29,7 @@
 //    (b, KV head) that lies in one share is written by it, the others' parts
 //    go to the caller's workspace and a second kernel joins them, in order.
 // Measured (D = 128): 24 sequences of up to 32768 rows, window 4096, bf16, 8 KV
-// heads: 56 us (6.5 TB/s); 8 sequences of 65536 to 131072 rows, 4 bits: 149 us
+// heads: 56 us (6.5 TB/s); 8 sequences of 65536 to 131072 rows, 4 bits: 150 us
 // (5.9 TB/s); one sequence, window 512: 4.7 us.
 //
 // 4-bit cache (layout: kv_int4.cu).  A nibble lined up under a mask is an fp16
@@ -69,10 +69,10 @@ constexpr int kClusterRows = 4096;
 // 4-bit cache: log2 of P's factor; pairs of fp16: the least and the most a group's bound may be (2^-14, 2^14), and
 // what a pair of powers of two is taken from for their inverses (the exponents mirrored)
 constexpr float kLift = 14.f;
+constexpr uint32_t kBoundLeast = 0x04000400u, kBoundMost = 0x74007400u, kPow2Inverse = 0x78007800u;
 // units of a warp after which the zeros' sums join the codes' (8 sequences of up to 131072 rows, flat scores: error
 // 0.0024 -> 0.0017, of which 0.0016 is the result's rounding, 156 -> 161 us; after 4 or 8 units no less)
 constexpr int kFold = 16;
-constexpr uint32_t kBoundLeast = 0x04000400u, kBoundMost = 0x74007400u, kPow2Inverse = 0x78007800u;
 
 // rows a sequence may see at most (the lengths are on the device)
 long long win_decode_rows(const WinDecodeArgs& a) {
