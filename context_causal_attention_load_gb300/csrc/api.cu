@@ -922,6 +922,10 @@ int check_win_attn(AttnShape& sh, int window, int sinks, Window& win) {
   if (sh.Dqk != 64 && sh.Dqk != 128)
     return fail(CPATTN_ERR_UNSUPPORTED, "windowed attention head dim %d not in {64, 128}", sh.Dqk);
   if ((rc = check_attn(sh))) return rc;
+  // (row statistics lie in whole tiles of 128, however short a chunk)
+  if ((long long)WinTiles::make(sh.S, sh.cp, sh.lb).nt * kTile > (1LL << 31) - 1)
+    return fail(CPATTN_ERR_UNSUPPORTED, "%d chunks of %d tokens exceed 2^31 rows of whole tiles", 2 * sh.cp,
+                sh.S / (2 * sh.cp));
   win.window = std::min(window, sh.S);
   win.sinks = std::min(sinks, sh.S);
   return CPATTN_OK;

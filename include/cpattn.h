@@ -286,7 +286,8 @@ int gqa_decode_noalloc(const void* q, const void* kcache, const void* vcache, co
  * original ones in every token order, so a model that alternates full and
  * windowed layers keeps its tensors in load-balanced order throughout.
  * Layouts, cp, load_balance, scale and constraints as cp_attn_fwd, with
- * D = Dqk = Dv in {64, 128}.  The rows of q, k, v must be finite, masked ones
+ * D = Dqk = Dv in {64, 128}, and below 2^24 chunks of fewer than 128 tokens.
+ * The rows of q, k, v must be finite, masked ones
  * too (a masked weight is a zero, and 0 * inf is NaN).
  */
 int cp_attn_fwd_window(const void* q, const void* k, const void* v, void* out, float* lse, int B, int Hq, int Hkv,
@@ -367,7 +368,8 @@ int kv_read_int4(const void* kcodes, const void* kparams, const void* vcodes, co
  * 2^-11 of themselves each time, whatever the size of the values: probability
  * times scale down to 2^-28 of the group's largest (or 2^-14, if that is more),
  * scales down to 2^-14 of it.
- * q and out [B, Hq, D] bf16; the rest as gqa_decode_window.
+ * Scores of up to 2^27 in magnitude.  q and out [B, Hq, D] bf16; the rest as
+ * gqa_decode_window.
  */
 int gqa_decode_int4(const void* q, const void* kcodes, const void* kparams, const void* vcodes, const void* vparams,
                     const int* lens, void* out, int B, int Hq, int Hkv, int Smax, int D, int window, int sinks,
