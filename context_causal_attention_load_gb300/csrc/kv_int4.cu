@@ -82,6 +82,36 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// what rounding a - b to d left: d and this are together exactly a - b (Knuth's TwoSum)
+__device__ __forceinline__ float rest_of_diff(float a, float b, float d) {
+  const float t = __fsub_rn(d, a);
+  return __fsub_rn(__fsub_rn(a, __fsub_rn(d, t)), __fadd_rn(b, t));
+}
+// (v - z) / s to the nearest whole number, ties to the even one, q being the quotient to a few 2^-24: whether to go up
+// from k = floor(q) is the sign of v - z - (k + 1/2) s.  Where the difference is not what fp32 makes of it (v far
+// smaller than z) its rest decides what looks like a tie: (k + 1/2) s is a multiple of the difference's last place.
+__device__ __forceinline__ int nearest_code(float v, float z, float s, float q) {
+  const float d = v - z, k = floorf(q);
+  float off = fmaf(-(k + 0.5f), s, d);
+  if (off == 0.f) off = rest_of_diff(v, z, d);
+  const int n = (int)k;
+  return n + (off > 0.f || (off == 0.f && (n & 1)) ? 1 : 0);
+}
+// fp16((hi - lo) / 15), rounded once: the difference and the quotient are rounded to odd (an inexact one gets an odd
+// last place, so that it lies on the same side of every fp16 and every midpoint as what it stands for).  This and the
+// next, the long way's, are calls: inlined they cost the others registers (4 x 8192 tokens: 46 us instead of 44).
+__device__ __noinline__ __half exact_scale(float hi, float lo) {
+  uint32_t d = __float_as_uint(hi - lo);
+  const float rest = rest_of_diff(hi, lo, hi - lo);
+  if (rest < 0.f) d -= 1;
+  if (rest != 0.f) d |= 1;
+  const float df = __uint_as_float(d), q = __fdiv_rz(df, 15.f);
+  const bool inexact = fmaf(-q, 15.f, df) != 0.f;
+  return __float2half_rn(__uint_as_float(__float_as_uint(q) | (inexact ? 1u : 0u)));
+}
+__device__ __noinline__ int clamped_code(float v, float z, float s) {
+  return min(max(nearest_code(v, z, s, (v - z) / s), 0), 15);
+}
 __device__ __forceinline__ float clamp_limit(float x) { return fminf(fmaxf(x, -kInt4Limit), kInt4Limit); }
 
 // Two lanes per group, sixteen channels each (32 bytes, a sector), so that a
@@ -182,7 +212,7 @@ __global__ void __launch_bounds__(kThreadsKv, 4) kv_append_int4_kernel(const __g
           !(fmaxf(mx, -mn) <= kInt4Limit)) {
         const bool bad = !(mx < INFINITY && mn > -INFINITY);  // a NaN or an infinity
         const float lo2 = clamp_limit(mn);
-        hs = bad ? __ushort_as_half(0x7fff) : __float2half_rn((clamp_limit(mx) - lo2) / 15.f);
+        hs = bad ? __ushort_as_half(0x7fff) : exact_scale(clamp_limit(mx), lo2);
         hz = bad ? __ushort_as_half(0x7fff) : __float2half_rn(lo2);
         const float s2 = __half2float(hs), z2 = __half2float(hz);
 #pragma unroll 1
@@ -191,20 +221,16 @@ __global__ void __launch_bounds__(kThreadsKv, 4) kv_append_int4_kernel(const __g
 #pragma unroll
           for (int i = 7; i >= 0; --i) {
             const uint32_t p = q ? x[4 + i / 2] : x[i / 2];
-            const float d = clamp_limit((i & 1) ? bf16hi(p) : bf16lo(p)) - z2;
-            v = (v << 4) + (uint32_t)(s2 > 0.f ? fminf(fmaxf(rintf(d / s2), 0.f), 15.f) : 0.f);
+            const float x1 = clamp_limit((i & 1) ? bf16hi(p) : bf16lo(p));
+            v = (v << 4) + (uint32_t)(s2 > 0.f ? clamped_code(x1, z2, s2) : 0);
           }
           if (q) w[1] = v;
           else w[0] = v;
         }
       } else if (min(near & 0xffffu, near >> 16) <= 6u) {
-        // the pairs that come close to a tie, exactly: x - zero against (k + 1/2) scale.  (The other of a pair may lie
-        // below zero, which is rounded where the least value is small: k is -1 then.)
-        auto code = [&](float v) {
-          const float d = v - z, k = floorf(d * inv), t = fmaf(-(k + 0.5f), s, d);
-          const int n = (int)k;
-          return (uint32_t)(n + (t > 0.f || (t == 0.f && (n & 1)) ? 1 : 0));
-        };
+        // the pairs that come close to a tie, exactly.  (The other of a pair may lie below zero, which is rounded where
+        // the least value is small, by less than half a scale: its code is 0.)
+        auto code = [&](float v) { return (uint32_t)nearest_code(v, z, s, (v - z) * inv); };
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll

@@ -69,3 +69,35 @@ def test_mixed_groups():
     x = torch.where(few, x * torch.exp2(torch.randint(-12, 3, x.shape, generator=g).float()), x)
     x[::7] = x[::7].abs() + x[::7].abs().amax(-1, keepdim=True) * 3  # far from zero
     _same(x.reshape(T, 1, D).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("power", [-23, -20, -14, -7, 0, 6, 11])
+def test_values_far_smaller_than_their_group(power):
+    """zeros half a step from a whole code, and values so much smaller that a difference in fp32 does not show them:
+    which side of the tie they lie on decides; groups with a clamped value among them"""
+    D, T = 128, 1024
+    g = torch.Generator().manual_seed(3000 + power)
+    half = torch.randint(0, 15, (T, 1, D // 32, 1), generator=g) + 0.5
+    tiny = torch.exp2(-torch.randint(18, 46, (T, 1, D // 32, 32), generator=g).float())
+    x = tiny * torch.randint(-1, 2, tiny.shape, generator=g)
+    x[..., 0], x[..., 1] = -half[..., 0], 15.0 - half[..., 0]
+    x = x * 2.0 ** power
+    if power == 11:
+        x[::2, ..., 1] = 1e6
+    _same(x.reshape(T, 1, D).to(torch.bfloat16))
+
+
+def test_scales_on_and_beside_ties():
+    """spans of 15 * (2m + 1) / 2 of fp16's least scale, and a hair more or less"""
+    D, T = 128, 512
+    g = torch.Generator().manual_seed(4000)
+    m = torch.randint(0, 8, (T, 1, D // 32, 1), generator=g)
+    x = torch.zeros(T, 1, D // 32, 32)
+    x[..., 5] = (15 * (2 * m + 1))[..., 0] * 2.0 ** -25
+    x[..., 9] = (torch.randint(-1, 2, (T, 1, D // 32), generator=g) * torch.exp2(-torch.randint(45, 60, (T, 1, D // 32), generator=g).float()))
+    x[..., 10:] = x[..., 5:6] * torch.randint(0, 17, (T, 1, D // 32, 22), generator=g) / 16
+    low = x[..., 9] > 0
+    x[..., :5] = torch.where(low[..., None], x[..., 9:10], x[..., :5])  # no zeros below a least value above zero
+    x[..., 6:9] = torch.where(low[..., None], x[..., 9:10], x[..., 6:9])
+    x[..., 10:] = torch.maximum(x[..., 10:], x[..., 9:10])
+    _same(x.reshape(T, 1, D).to(torch.bfloat16))
