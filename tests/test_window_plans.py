@@ -63,7 +63,7 @@ def test_any_number_of_shapes():
     for w in range(2, 1002):  # 1000 lists of 64 KB forward, and of 64 KB and more backward
         fwd(w)
         assert lib.cp_attn_bwd_window_workspace(B, H, H, S, D, 1, 0, w, 0, ctypes.byref(n), None) == 0
-    # 16 MB each, and what the driver takes memory in
+    # 16 MB each, and the pieces device memory comes in
     assert _grown(before) <= 40 << 20, _grown(before)
     same = lambda a, b: all(torch.equal(a[i], b[i]) for i in (0, 1, 3, 4))  # noqa: E731  (dq's sums vary in order)
     graph.replay()
